@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
       mbar_init(BAR(C::kBarPVDone + i), 1);
       mbar_init(BAR(C::kBarUnitFull + i), 1);
       mbar_init(BAR(C::kBarUnitEmpty + i), C::kUnitReaders);
-      mbar_init(BAR(C::kBarOStage + i), 1);
+      mbar_init(BAR(C::kBarOStage + i), 4);  // one arrive per softmax warp
       mbar_init(BAR(C::kBarOReady + i), 4);  // one arrive per softmax warp
       mbar_init(BAR(C::kBarOFree + i), 1);
       mbar_init(BAR(C::kBarPHalf + i), 4);  // one arrive per softmax warp
@@ -1028,7 +1028,10 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
     uint8_t* ostage = smem + C::kOffO;
     // The two tiles take turns with the one O staging buffer, in the order tile 0 of
     // unit 0, tile 1 of unit 0, tile 0 of unit 1, ...: a turn starts when the previous
-    // turn's TMA store has finished reading the buffer (an inactive tile passes its turn).
+    // turn's TMA store has finished reading the buffer (a tile without a store passes its turn).
+    // Every warp of the slot arrives for its turn once it has seen the turn before end: were one
+    // arrival enough, turns passed in a row (a slot whose tiles have no query or no key) could end
+    // a phase that a slower warp still waits for.
     auto ostage_acquire = [&](int k) {
       if (t == 0 && k > 0) mbar_wait_inline(BAR(C::kBarOStage + 1), (k - 1) & 1, wctx);
       if (t == 1) mbar_wait_inline(BAR(C::kBarOStage + 0), k & 1, wctx);
@@ -1052,7 +1055,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
       const int grow = row0 + r;  // global query row
       if (nkv == 0) {
         ostage_acquire(k);  // pass this tile's turn with the staging buffer
-        if (threadIdx.x == 128 * t) mbar_arrive(BAR(C::kBarOStage + t));
+        if (lane == 0) mbar_arrive(BAR(C::kBarOStage + t));
         // every row of this tile is left without a key (causal, Nq > Nk): O = 0, lse = -inf
         if (row0 < p.Nq && grow < p.Nq) {
           uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) +
@@ -1224,6 +1227,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
       fence_proxy_async_smem();  // generic-proxy writes -> visible to the TMA store
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(C::kBarOReady + t));
+      if (lane == 0 && quarter != 0) mbar_arrive(BAR(C::kBarOStage + t));
       if (quarter == 0) {
         mbar_wait_inline(BAR(C::kBarOReady + t), (no - 1) & 1, wctx);
         if (r == 0 && !*abort_flag) {
