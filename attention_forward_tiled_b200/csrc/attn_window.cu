@@ -288,13 +288,24 @@ int launch_window_bwd(const DeviceInfo& dev, const void* q, const void* k, const
   if (q_units >= (1LL << 31) || sink_units + rest_units >= (1LL << 31) || joined * kJoinBlocks >= (1LL << 31))
     return ATTN_ERR_INVALID_ARG;
 
-  const size_t dsum_bytes = ((size_t)B * H * Nq * 4 + 255) / 256 * 256;
+  const int n_kblocks = (Nk + 127) / 128;
+  const long long bound_blocks = heads * n_kblocks, n_qmax = 2 * heads * ((Nq + 127) / 128);
+  if (bound_blocks >= (1LL << 31)) return ATTN_ERR_INVALID_ARG;
+  const size_t dsum_bytes = ((size_t)B * H * Nq * 4 + 255) / 256 * 256, part_bytes = (size_t)parts * 256 * D * 4;
+  const size_t vmax_bytes = BF16 ? 0 : ((size_t)bound_blocks * 4 + 255) / 256 * 256;
   void* ws = nullptr;
-  if (int rc = take_workspace(dev, &ws, dsum_bytes + (size_t)parts * 256 * D * 4, stream)) return rc;
-  pq.dsum = pk.dsum = static_cast<float*>(ws);
-  pk.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + dsum_bytes);
-  attn_window_bwd_kernel<D, BF16, false><<<(unsigned)q_units, C::kThreads, C::kSmemBytes, stream>>>(pq);
-  int rc = launched();
+  if (int rc = take_workspace(dev, &ws, dsum_bytes + part_bytes + vmax_bytes + (BF16 ? 0 : n_qmax * 4), stream)) return rc;
+  uint8_t* at = static_cast<uint8_t*>(ws);
+  pq.dsum = pk.dsum = reinterpret_cast<float*>(at);
+  pk.part = reinterpret_cast<float*>(at + dsum_bytes);
+  pq.vmax = pk.vmax = reinterpret_cast<float*>(at + dsum_bytes + part_bytes);
+  pq.qmax = pk.qmax = reinterpret_cast<unsigned*>(at + dsum_bytes + part_bytes + vmax_bytes);
+  int rc = ATTN_OK;
+  if constexpr (!BF16) {
+    attn_window_bwd_kernel_bounds<D><<<(unsigned)bound_blocks, 256, 0, stream>>>(
+        v, reinterpret_cast<float*>(at + dsum_bytes + part_bytes), pq.qmax, Hkv, Nk, n_kblocks, n_qmax);
+    rc = launched();
+  }
   // The later launches may start while the one before ends (programmatic dependent launch); they
   // wait for its end before they read what it wrote.
   cudaLaunchAttribute early;
@@ -303,6 +314,13 @@ int launch_window_bwd(const DeviceInfo& dev, const void* q, const void* k, const
   cudaLaunchConfig_t cfg{};
   cfg.stream = stream;
   cfg.attrs = &early;
+  cfg.numAttrs = BF16 ? 0 : 1;
+  if (rc == ATTN_OK) {
+    cfg.gridDim = dim3((unsigned)q_units);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmemBytes;
+    if (cudaLaunchKernelEx(&cfg, attn_window_bwd_kernel<D, BF16, false>, pq) != cudaSuccess) rc = ATTN_ERR_CUDA;
+  }
   cfg.numAttrs = 1;
   if (rc == ATTN_OK) {
     cfg.gridDim = dim3((unsigned)(sink_units + rest_units));

@@ -27,6 +27,16 @@
 // times, so there dS enters as the sum of two 16-bit values (the second is what the first was
 // rounded by, in the half of T's columns that the first leaves free), a product each: 272 -> 327 us.
 //
+// Range: dS carries the size of dO and of V, and fp16 has 2^-24 to 2^16 (dO of 1e-3 left dQ and dK at 3
+// times their own rounding, dO V^T past 65504 gave NaN).  So in fp16 dS enters as 2^e dS, with e from a
+// bound of |T - D|, |dO| |v| + |D| (and P <= 1), that puts it below 2^14, and the gradient is taken back by
+// 2^-e: dQ's e is its row's, from |dO| of the row and the largest |v| among the unit's keys; dK's is the
+// unit's, from the largest |dO| and |D| of its queries, by 128 of them, which the queries' launch leaves
+// behind.  Typical products lie 2^4 to 2^8 below the bound, so P down to 2^-17 and rows of 2^-10 of the
+// largest still enter as normal numbers.  P enters dV as 2^12 P.  The powers of two ride in the exponent
+// of P and in the subtraction of D; what they cost is the bounds (a small launch over V, and some 0.5 us a
+// unit): 4096 tokens in fp16 640 -> 667 us, 1000 tokens 37.2 -> 40.3.  bf16 has fp32's range and none of it.
+//
 // What bounds it, at 4096 tokens of 2 x 32 heads over 8, 128 channels, window 1024: the queries'
 // launch takes 327 us, the keys' 313, the join 6; the tensor cores work 40 and 46 % of that, the
 // issue slots 36 and 29 %, DRAM 11 %.  A unit is 9 or 10 steps and about 5 us of them its start and
@@ -58,6 +68,9 @@ struct WindowBwdParams {
   void* g1;                  // dQ | dV
   void* g2;                  // - | dK
   float* part;               // the keys' launch: [parts][2][128][D] of split units
+  const float* vmax;         // fp16: [B, Hkv, ceil(Nk / 128)]: largest |v|^2 of 128 keys, and
+  unsigned* qmax;            // [B, Hkv, ceil(Nq / 128)][2]: largest |dO| (a bound of it) and |D| of 128
+                             // queries, as bits of floats that are not negative
   int* status;
   int B, H, Hkv, Nq, Nk;
   int lg_pack;               // the queries' launch
@@ -86,7 +99,8 @@ struct WindowBwdCfg {
   static constexpr int kUnitInts = 8;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;    // tmem slot, abort flag, unit slots
   static constexpr int kOffClc = (kOffMisc + 8 + 2 * kUnitInts * 4 + 15) / 16 * 16;
-  static constexpr int kSmemBytes = kOffClc + 16;            // the shared memory is declared 1 KB aligned
+  static constexpr int kOffNorm = kOffClc + 16;              // queries, fp16: uint8 [4][128], quarters of |dO|^2
+  static constexpr int kSmemBytes = kOffNorm + 512;          // the shared memory is declared 1 KB aligned
   static constexpr int kEwWarps = 16, kProducerWarp = 16, kMmaWarp = 17, kThreads = 576;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
@@ -158,6 +172,58 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ uint64_t f2_bits(uint32_t lo, uint32_t hi) {
   return f2_make(__uint_as_float(lo), __uint_as_float(hi));
+}
+
+// fp16: P of the keys' launch enters the products as 2^kPShift P, and dS as 2^e dS.
+constexpr int kPShift = 12;
+// e for |T - D| <= bound: 2^e bound lies in [2^13, 2^14).  (fp16 inputs: nonzero bounds lie in [2^-49, 2^42].)
+__device__ __forceinline__ int ds_shift(float bound) {
+  return min(max(13 - ((int)(__float_as_uint(bound) >> 23) - 127), -64), 64);
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+__device__ __forceinline__ float warp_max(float x) {  // of values that are not negative
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
+}
+
+// fp16, before the queries' launch: the largest |v|^2 of each 128 keys of a head (a block each), and
+// qmax set to 0.
+template <int D>
+__global__ void __launch_bounds__(256) attn_window_bwd_kernel_bounds(const void* v, float* vmax, unsigned* qmax, int Hkv,
+                                                                     int Nk, int n_kblocks, long long n_qmax) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  constexpr int kLanes = D / 8, kPasses = 128 * kLanes / 256;  // lanes of a row; rows of a thread
+  __shared__ unsigned top;
+  if (threadIdx.x == 0) top = 0u;
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n_qmax; i += gridDim.x * 256LL) qmax[i] = 0u;
+  const int bh = blockIdx.x / n_kblocks, key0 = 128 * (blockIdx.x - bh * n_kblocks);
+  const int b = bh / Hkv, hk = bh - b * Hkv;
+  const int row = threadIdx.x / kLanes, c = threadIdx.x % kLanes;
+  uint4 x[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int key = key0 + row + i * (256 / kLanes);
+    x[i] = key < Nk ? __ldg(static_cast<const uint4*>(v) + (((long long)b * Nk + key) * Hkv + hk) * kLanes + c)
+                    : make_uint4(0u, 0u, 0u, 0u);
+  }
+  float most = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = unpack2<false>(w[e]);
+      s = fmaf(f.x, f.x, fmaf(f.y, f.y, s));
+    }
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    most = fmaxf(most, s);
+  }
+  most = warp_max(most);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) atomicMax(&top, __float_as_uint(most));
+  __syncthreads();
+  if (threadIdx.x == 0) vmax[blockIdx.x] = __uint_as_float(top);
 }
 
 template <int D, bool BF16, bool kKeys>
@@ -448,7 +514,8 @@ __global__ void __launch_bounds__(WindowBwdCfg<D>::kThreads, 1)
     const long long diag = (long long)p.Nk - p.Nq;
     const float cs = p.scale_log2;
     float* rowbuf = reinterpret_cast<float*>(smem + C::kOffRow);
-    if constexpr (kKeys) asm volatile("griddepcontrol.wait;" ::: "memory");  // D has been written
+    // what the launch before wrote: keys: D; fp16: the bounds
+    if constexpr (kKeys || !BF16) asm volatile("griddepcontrol.wait;" ::: "memory");
     int g = 0, nx = 0;  // steps and units with steps so far
     WindowBwdUnit u = next_unit(0);
     // Of the unit that u is: this lane's row of the X tiles, and what is loaded of it ahead, while
@@ -461,6 +528,8 @@ __global__ void __launch_bounds__(WindowBwdCfg<D>::kThreads, 1)
     // keys: lse and D of the step's columns, by one warp of the four that share them, a step ahead
     const bool row_warp = kKeys && (warp & 3) == 0;
     float nl = 0.f, nd = 0.f;
+    // fp16: this lane's share of the largest |v|^2 of the unit's keys; keys: of |dO| and |D| of its queries
+    float v_most = 0.f, g_most = 0.f, d_most = 0.f;
     auto load_row = [&](int hd, int qt) {  // head of the group and query tile
       const int q = u.a + 128 * qt + part * 32 + lane;
       const long long at = ((long long)u.b * p.H + u.h * G + hd) * p.Nq + q;
@@ -472,6 +541,27 @@ __global__ void __launch_bounds__(WindowBwdCfg<D>::kThreads, 1)
       head = kKeys ? u.h : u.h + (r & ((1 << p.lg_pack) - 1));
       valid = xrow < (kKeys ? p.Nk : p.Nq);
       if (u.n <= 0) return;
+      if constexpr (!BF16) {
+        const long long bh = (long long)u.b * p.Hkv + (kKeys ? u.h : u.h / G);
+        const float* vm = p.vmax + bh * ((p.Nk + 127) / 128);
+        v_most = 0.f;
+        if constexpr (kKeys) {
+          v_most = __ldcg(vm + u.x0 / 128);
+          g_most = d_most = 0.f;
+          const float2* qm = reinterpret_cast<const float2*>(p.qmax) + bh * ((p.Nq + 127) / 128);
+          const int last = (int)min((long long)p.Nq, u.a + 128LL * u.c) - 1;
+          for (int i = u.a / 128 + lane; i <= last / 128; i += 32) {
+            const float2 w = __ldcg(qm + i);
+            g_most = fmaxf(g_most, w.x);
+            d_most = fmaxf(d_most, w.y);
+          }
+        } else {
+          // the sinks (rows of the stream below a), then keys from a + c on
+          const int last = (int)min((long long)p.Nk, 128LL * u.n + u.c) - 1;
+          for (int i = lane; i < (min(u.a, p.Nk) + 127) / 128; i += 32) v_most = fmaxf(v_most, __ldcg(vm + i));
+          for (int i = (u.a + u.c) / 128 + lane; i <= last / 128; i += 32) v_most = fmaxf(v_most, __ldcg(vm + i));
+        }
+      }
       if constexpr (kKeys) {
         if (row_warp) load_row(u.s0 / u.c, u.s0 % u.c);
       } else {
@@ -490,6 +580,16 @@ __global__ void __launch_bounds__(WindowBwdCfg<D>::kThreads, 1)
         lse2 *= 1.4426950408889634f;
         if (valid && u.n == 0 && part == 0)  // a row that sees no key
           p.dsum[((long long)u.b * p.H + head) * p.Nq + xrow] = 0.f;
+      }
+      // fp16: dS enters its product as 2^e dS; keys: T and D times f1, dS = P' f1 (T - D)
+      [[maybe_unused]] float f1 = 1.f, undo = 1.f;
+      if constexpr (!BF16) {
+        v_most = warp_max(v_most);
+        if constexpr (kKeys) {
+          const int e = ds_shift(fmaf(warp_max(g_most), sqrtf(v_most), warp_max(d_most)));
+          f1 = pow2(e - kPShift);
+          undo = pow2(-e);
+        }
       }
       // what this lane sees: keys: queries [see_lo, see_hi); queries: keys as WindowRow
       int see_lo = 0, see_hi = 0, see_sink = 0;
@@ -520,8 +620,8 @@ __global__ void __launch_bounds__(WindowBwdCfg<D>::kThreads, 1)
           see = bits(u.a + 128 * qt);
           float* buf = rowbuf + (g & 1) * 256 + part * 32;
           if (row_warp) {
-            buf[lane] = -nl;
-            buf[128 + lane] = -nd;
+            buf[lane] = BF16 ? -nl : (float)kPShift - nl;
+            buf[128 + lane] = BF16 ? -nd : -nd * f1;
           }
           if (++qt == u.c) {
             qt = 0;
@@ -539,6 +639,50 @@ __global__ void __launch_bounds__(WindowBwdCfg<D>::kThreads, 1)
           }
         }
         const bool all = __all_sync(0xffffffffu, see == 0xffffffffu);
+        if (!kKeys && i == 0) {
+          // D of the row: this warp's quarter of its channels, joined through shared memory (the
+          // unit before has ended: every warp has read its D)
+          mbar_wait_inline(BAR(C::kBarXFull + 1), nx & 1, wctx);
+          __syncwarp();
+          const uint8_t* dO = smem + C::kTile;
+          float s = 0.f, n2 = 0.f;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            const int chunk = part * (D / 32) + c;
+            const uint4 v = *reinterpret_cast<const uint4*>(dO + (chunk >> 3) * C::kBox + r * 128 +
+                                                            (((chunk & 7) ^ (r & 7)) << 4));
+            const uint32_t a4[4] = {orow[c].x, orow[c].y, orow[c].z, orow[c].w}, b4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 fa = unpack2<BF16>(a4[e]), fb = unpack2<BF16>(b4[e]);
+              s = fmaf(fa.x, fb.x, fmaf(fa.y, fb.y, s));
+              if constexpr (!BF16) n2 = fmaf(fb.x, fb.x, fmaf(fb.y, fb.y, n2));
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(BAR(C::kBarXEmpty + 1));
+          rowbuf[part * 128 + r] = s;
+          [[maybe_unused]] uint8_t* norm = smem + C::kOffNorm;  // |dO|^2 of a quarter is below 2^(norm - 126)
+          if constexpr (!BF16) norm[part * 128 + r] = (uint8_t)(__float_as_uint(n2) >> 23);
+          meet(BAR(C::kBarMeet), nx, wctx);
+          dd = (rowbuf[r] + rowbuf[128 + r]) + (rowbuf[256 + r] + rowbuf[384 + r]);
+          if (valid && part == 0) p.dsum[row_at] = dd;
+          if constexpr (!BF16) {
+            n2 = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) n2 += pow2((int)norm[i * 128 + r] - 126);
+            const float size = sqrtf(n2);
+            const int e = ds_shift(fmaf(size, sqrtf(v_most), fabsf(dd)));
+            undo = pow2(-e);
+            lse2 -= (float)e;  // P comes out as 2^e P
+            if (part == 0) {
+              const float top_n = warp_max(size), top_d = warp_max(fabsf(dd));
+              if (lane < 2)
+                atomicMax(p.qmax + 2 * (((long long)u.b * p.Hkv + u.h / G) * ((p.Nq + 127) / 128) + u.x0 / 128) + lane,
+                          __float_as_uint(lane ? top_d : top_n));
+            }
+          }
+        }
         // ---- P
         mbar_wait_inline(BAR(C::kBarS), g & 1, wctx);
         __syncwarp();
@@ -582,31 +726,6 @@ __global__ void __launch_bounds__(WindowBwdCfg<D>::kThreads, 1)
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(BAR(C::kBarP));
-        } else if (i == 0) {
-          // D of the row: this warp's quarter of its channels, joined through shared memory (the
-          // unit before has ended: every warp has read its D)
-          mbar_wait_inline(BAR(C::kBarXFull + 1), nx & 1, wctx);
-          __syncwarp();
-          const uint8_t* dO = smem + C::kTile;
-          float s = 0.f;
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            const int chunk = part * (D / 32) + c;
-            const uint4 v = *reinterpret_cast<const uint4*>(dO + (chunk >> 3) * C::kBox + r * 128 +
-                                                            (((chunk & 7) ^ (r & 7)) << 4));
-            const uint32_t a4[4] = {orow[c].x, orow[c].y, orow[c].z, orow[c].w}, b4[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 fa = unpack2<BF16>(a4[e]), fb = unpack2<BF16>(b4[e]);
-              s = fmaf(fa.x, fb.x, fmaf(fa.y, fb.y, s));
-            }
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(BAR(C::kBarXEmpty + 1));
-          rowbuf[part * 128 + r] = s;
-          meet(BAR(C::kBarMeet), nx, wctx);
-          dd = (rowbuf[r] + rowbuf[128 + r]) + (rowbuf[256 + r] + rowbuf[384 + r]);
-          if (valid && part == 0) p.dsum[row_at] = dd;
         }
         // ---- dS
         const uint32_t tT = tS + (!kKeys && (g & 1) ? 384 : 128);
@@ -626,7 +745,9 @@ __global__ void __launch_bounds__(WindowBwdCfg<D>::kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
               if constexpr (kKeys) d2 = e ? f2_make(d4.z, d4.w) : f2_make(d4.x, d4.y);
-              const float2 ds = f2_split(f2_mul(f2_make(pr[c + e], pr[c + e + 1]), f2_add(f2_bits(t[c + e], t[c + e + 1]), d2)));
+              const uint64_t td = kKeys && !BF16 ? f2_fma(f2_bits(t[c + e], t[c + e + 1]), f2_make(f1, f1), d2)
+                                                 : f2_add(f2_bits(t[c + e], t[c + e + 1]), d2);
+              const float2 ds = f2_split(f2_mul(f2_make(pr[c + e], pr[c + e + 1]), td));
               w[(c + e) / 2] = pack2<BF16>(ds.x, ds.y);
               if constexpr (!kKeys) {
                 const float2 hi = unpack2<BF16>(w[(c + e) / 2]);
@@ -668,17 +789,19 @@ __global__ void __launch_bounds__(WindowBwdCfg<D>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e) a[e] = b[e] = 0u;
         }
+        // what dQ | dV and dK are to be multiplied by (but for the scale, of parts of dK)
+        const float by1 = kKeys ? (BF16 ? 1.f : pow2(-kPShift)) : p.scale * undo;
         if (kKeys && done.part >= 0) {
           float4* dst = reinterpret_cast<float4*>(p.part + ((long long)done.part * 256 + r) * D + c * 16);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            dst[e] = make_float4(__uint_as_float(a[4 * e]), __uint_as_float(a[4 * e + 1]), __uint_as_float(a[4 * e + 2]),
-                                 __uint_as_float(a[4 * e + 3]));
-            dst[32 * D + e] = make_float4(__uint_as_float(b[4 * e]), __uint_as_float(b[4 * e + 1]),
-                                          __uint_as_float(b[4 * e + 2]), __uint_as_float(b[4 * e + 3]));
+            dst[e] = make_float4(__uint_as_float(a[4 * e]) * by1, __uint_as_float(a[4 * e + 1]) * by1,
+                                 __uint_as_float(a[4 * e + 2]) * by1, __uint_as_float(a[4 * e + 3]) * by1);
+            dst[32 * D + e] = make_float4(__uint_as_float(b[4 * e]) * undo, __uint_as_float(b[4 * e + 1]) * undo,
+                                          __uint_as_float(b[4 * e + 2]) * undo, __uint_as_float(b[4 * e + 3]) * undo);
           }
         } else if (store) {
-          const float f1 = kKeys ? 1.f : p.scale;
+          const float by2 = p.scale * undo;
           uint4* d1 = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.g1) + row + c * 16);
           uint4* d2 = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.g2) + row + c * 16);
 #pragma unroll
@@ -686,13 +809,12 @@ __global__ void __launch_bounds__(WindowBwdCfg<D>::kThreads, 1)
             uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              w[i] = pack2<BF16>(__uint_as_float(a[8 * e + 2 * i]) * f1, __uint_as_float(a[8 * e + 2 * i + 1]) * f1);
+              w[i] = pack2<BF16>(__uint_as_float(a[8 * e + 2 * i]) * by1, __uint_as_float(a[8 * e + 2 * i + 1]) * by1);
             d1[e] = make_uint4(w[0], w[1], w[2], w[3]);
             if constexpr (kKeys) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                w[i] = pack2<BF16>(__uint_as_float(b[8 * e + 2 * i]) * p.scale,
-                                   __uint_as_float(b[8 * e + 2 * i + 1]) * p.scale);
+                w[i] = pack2<BF16>(__uint_as_float(b[8 * e + 2 * i]) * by2, __uint_as_float(b[8 * e + 2 * i + 1]) * by2);
               d2[e] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }

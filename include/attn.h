@@ -366,6 +366,12 @@ ATTN_API int attn_fwd_window(const void* q, const void* k, const void* v, void* 
  *   any input.  A row that sees no key has a zero gradient, and so has a key that no query
  *   sees.  Every sum has a fixed order: equal calls give equal bits.  The workspace is taken
  *   stream-ordered from a pool that keeps up to 256 MiB between calls.
+ *
+ * P and dS enter their products rounded to dtype, dS of dQ in two parts: dq is off by little more
+ * than its own rounding, dk and dv by about 1.4 times theirs (root mean square).  In float16 both are
+ * moved by powers of two taken from |dout|, |v| and D, so this holds for small and large dout and v
+ * alike, as long as the gradients themselves lie in float16's normal range; queries whose dout is below
+ * 2^-10 of the largest of the 128 around them add to dk with fewer bits.
  * Returns ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED or ATTN_ERR_CUDA;
  * asynchronous like attn_fwd.
  */
