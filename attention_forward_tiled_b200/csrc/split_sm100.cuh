@@ -255,7 +255,8 @@ constexpr float kNoMax = -1e30f;
 // Counts a part of an item in; true for the last of n.  The word comes from a memory pool with
 // anything in it: a count is one only under the launch's nonce (48 random bits, so that a word
 // left by others passes for it once in 2^48), and the last part clears the word, so that a
-// replayed launch with the same nonce starts afresh.
+// replayed launch with the same nonce starts afresh.  So every part is counted in, those of a CTA
+// that gives up too: a count left behind would make the replay take an early part for the last.
 __device__ __forceinline__ bool split_arrive(unsigned long long* word, unsigned long long nonce, int n) {
   // the last part's guess is right at once, the others' time does not count
   unsigned long long seen = nonce | (unsigned long long)(n - 1);
@@ -964,7 +965,16 @@ __global__ void __launch_bounds__(256, SplitCfg<D, Q4, NT>::kCtas)
     run += cb - ca;
     fence_proxy_async_smem();  // the partials' shared memory becomes the ring again
     // one decision for the block: a warp alone that saw the abort would leave the others waiting
-    if (__syncthreads_or(run >= run_end || *abort_flag)) break;
+    if (__syncthreads_or(run >= run_end || *abort_flag)) {
+      if (run < run_end && warp == 0) {
+        // given up: of the items left only the last can go on in other CTAs; its part here is counted in
+        const SplitPlace at = split_find<D, Q4, NT>(p, run_end - 1);
+        const long long x0 = run_end - 1 - (run_end - 1 - at.begin) % at.n;
+        if (lane == 0 && x0 + at.n > run_end)
+          split_arrive(p.arrived + blockIdx.x, p.nonce, (int)((x0 + at.n - 1) / run_length) - (int)blockIdx.x + 1);
+      }
+      break;
+    }
     if (run >= place.begin + (long long)n_chunks * p.Hkv * p.row_chunks) {  // the next request that has keys
       place.begin = run;
       do ++place.b;
