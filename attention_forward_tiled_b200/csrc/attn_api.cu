@@ -66,13 +66,13 @@ std::mutex g_noalloc_mutex;
 
 int noalloc_scratch_ptr(float** out) {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cuda_failed();
   if (dev < 0 || dev >= kMaxDevices) return ATTN_ERR_UNSUPPORTED;
   std::lock_guard<std::mutex> lock(g_noalloc_mutex);
   if (g_noalloc_scratch_ptr[dev] == nullptr) {
     void* ptr = nullptr;
     if (cudaGetSymbolAddress(&ptr, g_noalloc_scratch) != cudaSuccess || ptr == nullptr)
-      return ATTN_ERR_CUDA;
+      return cuda_failed();
     g_noalloc_scratch_ptr[dev] = static_cast<float*>(ptr);
   }
   *out = g_noalloc_scratch_ptr[dev];
@@ -101,7 +101,7 @@ EncodeTiledFn get_encode_fn() {
 // Probe the current device once: sm_100 check, SM count, status-word address.
 int device_state(DeviceState** out) {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cuda_failed();
   if (dev < 0 || dev >= kMaxDevices) return ATTN_ERR_UNSUPPORTED;
   std::lock_guard<std::mutex> lock(g_dev_mutex);
   DeviceState& s = g_dev[dev];
@@ -110,12 +110,12 @@ int device_state(DeviceState** out) {
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-      return ATTN_ERR_CUDA;
+      return cuda_failed();
     s.supported = (major == 10 && minor == 0);
     s.sm_count = sms;
     if (s.supported) {
       void* ptr = nullptr;
-      if (cudaGetSymbolAddress(&ptr, g_attn_status) != cudaSuccess) return ATTN_ERR_CUDA;
+      if (cudaGetSymbolAddress(&ptr, g_attn_status) != cudaSuccess) return cuda_failed();
       s.status_ptr = static_cast<int*>(ptr);
     }
     s.probed = true;
@@ -132,7 +132,7 @@ int ensure_smem_attr(DeviceState* ds, int slot, Kernel kernel, int bytes) {
   if (ds->attr_set[slot]) return ATTN_OK;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
       cudaSuccess)
-    return ATTN_ERR_CUDA;
+    return cuda_failed();
   ds->attr_set[slot] = true;
   return ATTN_OK;
 }
@@ -141,7 +141,7 @@ int ensure_smem_attr(DeviceState* ds, int slot, Kernel kernel, int bytes) {
 int encode_bnhd(CUtensorMap* map, const void* ptr, int B, int N, int H, int d, int dtype,
                 int box_rows = 128, int box_heads = 1) {
   EncodeTiledFn encode = get_encode_fn();
-  if (!encode) return ATTN_ERR_CUDA;
+  if (!encode) return cuda_failed();
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)N, (cuuint64_t)B};
   const cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)H * d * 2,
                                  (cuuint64_t)N * H * d * 2};
@@ -159,7 +159,7 @@ int encode_bnhd(CUtensorMap* map, const void* ptr, int B, int N, int H, int d, i
 int encode_rows3d(CUtensorMap* map, const void* ptr, int B, long long rows, int d, int dtype,
                   int box_rows = 128) {
   EncodeTiledFn encode = get_encode_fn();
-  if (!encode) return ATTN_ERR_CUDA;
+  if (!encode) return cuda_failed();
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)B};
   const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)rows * d * 2};
   const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
@@ -176,7 +176,7 @@ int encode_rows3d(CUtensorMap* map, const void* ptr, int B, long long rows, int 
 // no swizzle (the backward's dQ accumulator, written by TMA reduce-adds).
 int encode_f32_bnhd(CUtensorMap* map, void* ptr, int B, int N, int H, int d, int box_rows) {
   EncodeTiledFn encode = get_encode_fn();
-  if (!encode) return ATTN_ERR_CUDA;
+  if (!encode) return cuda_failed();
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)N, (cuuint64_t)B};
   const cuuint64_t strides[3] = {(cuuint64_t)d * 4, (cuuint64_t)H * d * 4, (cuuint64_t)N * H * d * 4};
   const cuuint32_t box[4] = {(cuuint32_t)d, 1, (cuuint32_t)box_rows, 1};
@@ -191,7 +191,7 @@ int encode_f32_bnhd(CUtensorMap* map, void* ptr, int B, int N, int H, int d, int
 // swizzle.  Needs P a multiple of 8 (16-byte row pitch) and a 16-byte aligned base.
 int encode_mask3d(CUtensorMap* map, const void* ptr, int B, int T, int P, int box_tokens) {
   EncodeTiledFn encode = get_encode_fn();
-  if (!encode) return ATTN_ERR_CUDA;
+  if (!encode) return cuda_failed();
   const cuuint64_t dims[3] = {(cuuint64_t)P, (cuuint64_t)T, (cuuint64_t)B};
   const cuuint64_t strides[2] = {(cuuint64_t)P * 2, (cuuint64_t)T * P * 2};
   const cuuint32_t box[3] = {256, (cuuint32_t)box_tokens, 1};
@@ -272,7 +272,7 @@ int launch_prefill(DeviceState* ds, const void* q, const void* k, const void* v,
   const long long units = pairs + p.n_split;
   if (units >= (1LL << 31)) return ATTN_ERR_INVALID_ARG;
   kernel<<<dim3((unsigned)units), dim3(C::kThreads), C::kSmemBytes, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : cuda_failed();
 }
 
 // Split count for the decode kernel: minimise the largest per-CTA tile count
@@ -320,7 +320,7 @@ int launch_decode(DeviceState* ds, const void* q, const void* k, const void* v, 
   float* part = nullptr;
   const size_t ws_bytes = (size_t)items * (D + 2) * sizeof(float);
   if (cudaMallocAsync(reinterpret_cast<void**>(&part), ws_bytes, stream) != cudaSuccess)
-    return ATTN_ERR_CUDA;
+    return cuda_failed();
   p.q = q;
   p.part = part;
   p.status = ds->status_ptr;
@@ -334,13 +334,13 @@ int launch_decode(DeviceState* ds, const void* q, const void* k, const void* v, 
   p.timeout_ns = g_timeout_ns.load();
   const int grid = (int)std::min<long long>(items, ds->sm_count);
   kernel<<<dim3(grid), dim3(C::kThreads), C::kSmemBytes, stream>>>(p);
-  int rc = cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  int rc = cudaGetLastError() == cudaSuccess ? ATTN_OK : cuda_failed();
   if (rc == ATTN_OK) {
     attn_decode_combine_kernel<D, BF16>
         <<<dim3((unsigned)((BH + 3) / 4)), dim3(128), 0, stream>>>(part, out, lse, (int)BH, splits);
-    rc = cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    rc = cudaGetLastError() == cudaSuccess ? ATTN_OK : cuda_failed();
   }
-  if (cudaFreeAsync(part, stream) != cudaSuccess) rc = ATTN_ERR_CUDA;
+  if (cudaFreeAsync(part, stream) != cudaSuccess) rc = cuda_failed();
   return rc;
 }
 
@@ -373,7 +373,7 @@ int launch_decode_paged(DeviceState* ds, const void* q, const void* k_cache, con
   float* part = nullptr;
   const size_t ws_bytes = (size_t)items * (D + 2) * sizeof(float);
   if (cudaMallocAsync(reinterpret_cast<void**>(&part), ws_bytes, stream) != cudaSuccess)
-    return ATTN_ERR_CUDA;
+    return cuda_failed();
   p.q = q;
   p.part = part;
   p.status = ds->status_ptr;
@@ -393,13 +393,13 @@ int launch_decode_paged(DeviceState* ds, const void* q, const void* k_cache, con
   p.num_blocks = num_blocks;
   const int grid = (int)std::min<long long>(items, ds->sm_count);
   kernel<<<dim3(grid), dim3(C::kThreads), C::kSmemBytes, stream>>>(p);
-  int rc = cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  int rc = cudaGetLastError() == cudaSuccess ? ATTN_OK : cuda_failed();
   if (rc == ATTN_OK) {
     attn_decode_combine_kernel<D, BF16>
         <<<dim3((unsigned)((BH + 3) / 4)), dim3(128), 0, stream>>>(part, out, lse, (int)BH, splits);
-    rc = cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    rc = cudaGetLastError() == cudaSuccess ? ATTN_OK : cuda_failed();
   }
-  if (cudaFreeAsync(part, stream) != cudaSuccess) rc = ATTN_ERR_CUDA;
+  if (cudaFreeAsync(part, stream) != cudaSuccess) rc = cuda_failed();
   return rc;
 }
 
@@ -471,7 +471,7 @@ int launch_mq(DeviceState* ds, const void* q, const void* k_cache, const void* v
   float* part = nullptr;
   const size_t ws_bytes = (size_t)items * Lq * (D + 2) * sizeof(float);
   if (cudaMallocAsync(reinterpret_cast<void**>(&part), ws_bytes, stream) != cudaSuccess)
-    return ATTN_ERR_CUDA;
+    return cuda_failed();
   p.part = part;
   p.status = ds->status_ptr;
   p.B = B;
@@ -492,14 +492,14 @@ int launch_mq(DeviceState* ds, const void* q, const void* k_cache, const void* v
   p.num_blocks = num_blocks;
   const int grid = (int)std::min<long long>(items, ds->sm_count);
   kernel<<<dim3(grid), dim3(C::kThreads), C::kSmemBytes, stream>>>(p);
-  int rc = cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  int rc = cudaGetLastError() == cudaSuccess ? ATTN_OK : cuda_failed();
   if (rc == ATTN_OK) {
     const long long rows = BH * Lq;
     attn_mq_combine_kernel<D, BF16><<<dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream>>>(
         part, out, lse, B, H, Lq, splits);
-    rc = cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    rc = cudaGetLastError() == cudaSuccess ? ATTN_OK : cuda_failed();
   }
-  if (cudaFreeAsync(part, stream) != cudaSuccess) rc = ATTN_ERR_CUDA;
+  if (cudaFreeAsync(part, stream) != cudaSuccess) rc = cuda_failed();
   return rc;
 }
 
@@ -542,7 +542,7 @@ int launch_indexer(DeviceState* ds, const void* q, const void* kp, const float* 
   const int grid = (int)std::min<long long>(items, ds->sm_count);
   const int per_cta = (int)((items + grid - 1) / grid);
   kernel<<<dim3(grid), dim3(C::kThreads), C::kSmemBytes, stream>>>(p, per_cta);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : cuda_failed();
 }
 
 
@@ -578,7 +578,7 @@ int launch_relpos(DeviceState* ds, const void* q, const void* k, const void* v, 
   p.n_units = (int)units;
   const int grid = (int)std::min<long long>(units, ds->sm_count);  // persistent CTAs
   kernel<<<dim3(grid), dim3(C::kThreads), C::kSmemBytes, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : cuda_failed();
 }
 
 // Backward: D = rowsum(dO o O) and a zeroed fp32 dQ accumulator, the tiled gradient
@@ -602,12 +602,12 @@ int launch_bwd(DeviceState* ds, const void* q, const void* k, const void* v, con
   const size_t dsum_bytes = ((size_t)rows * 4 + 255) / 256 * 256;
   const size_t ws_bytes = dsum_bytes + (size_t)rows * D * 4;
   uint8_t* ws = nullptr;
-  if (cudaMallocAsync(reinterpret_cast<void**>(&ws), ws_bytes, stream) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (cudaMallocAsync(reinterpret_cast<void**>(&ws), ws_bytes, stream) != cudaSuccess) return cuda_failed();
   float* dsum = reinterpret_cast<float*>(ws);
   float* dq_acc = reinterpret_cast<float*>(ws + dsum_bytes);
   if (encode_f32_bnhd(&p.tm_dq, dq_acc, B, Nq, H, D, 64) != ATTN_OK) {
     cudaFreeAsync(ws, stream);
-    return ATTN_ERR_CUDA;
+    return cuda_failed();
   }
   p.lse = lse;
   p.dsum = dsum;
@@ -630,18 +630,18 @@ int launch_bwd(DeviceState* ds, const void* q, const void* k, const void* v, con
   if (rc == ATTN_OK) {
     attn_bwd_pre_kernel<D, BF16><<<dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream>>>(
         o, dout, dsum, dq_acc, B, H, Nq);
-    if (cudaGetLastError() != cudaSuccess) rc = ATTN_ERR_CUDA;
+    if (cudaGetLastError() != cudaSuccess) rc = cuda_failed();
   }
   if (rc == ATTN_OK) {
     kernel<<<dim3((unsigned)ctas), dim3(C::kThreads), C::kSmemBytes, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) rc = ATTN_ERR_CUDA;
+    if (cudaGetLastError() != cudaSuccess) rc = cuda_failed();
   }
   if (rc == ATTN_OK) {
     const long long n2 = rows * D / 2;
     attn_bwd_dq_kernel<BF16><<<dim3((unsigned)((n2 + 255) / 256)), dim3(256), 0, stream>>>(dq_acc, dq, n2, scale);
-    if (cudaGetLastError() != cudaSuccess) rc = ATTN_ERR_CUDA;
+    if (cudaGetLastError() != cudaSuccess) rc = cuda_failed();
   }
-  if (cudaFreeAsync(ws, stream) != cudaSuccess) rc = ATTN_ERR_CUDA;
+  if (cudaFreeAsync(ws, stream) != cudaSuccess) rc = cuda_failed();
   return rc;
 }
 
@@ -685,10 +685,10 @@ int launch_decode_noalloc(DeviceState* ds, const void* q, const void* k, const v
   p.timeout_ns = g_timeout_ns.load();
   const int grid = (int)std::min<long long>(items, ds->sm_count);
   kernel<<<dim3(grid), dim3(C::kThreads), C::kSmemBytes, stream>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess) return cuda_failed();
   attn_decode_combine_kernel<D, BF16>
       <<<dim3((unsigned)((BH + 3) / 4)), dim3(128), 0, stream>>>(part, out, lse, (int)BH, splits);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : cuda_failed();
 }
 
 int dispatch_prefill(DeviceState* ds, const void* q, const void* k, const void* v, void* out,
@@ -943,20 +943,20 @@ int attn_topk(const float* score, int R, int P, int k, int* idx, attn_stream_t s
       return rc;
     attn_topk_kernel<false><<<dim3(R), dim3(kTopkThreads), smem, st>>>(score, R, P, k, idx);
   }
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : cuda_failed();
 }
 
 int attn_get_status(attn_stream_t stream) {
   DeviceState* ds = nullptr;
   if (int rc = device_state(&ds)) return rc;
   if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return ATTN_ERR_CUDA;
+    return cuda_failed();
   int value = 0;
   if (cudaMemcpy(&value, ds->status_ptr, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
-    return ATTN_ERR_CUDA;
+    return cuda_failed();
   const int zero = 0;
   if (cudaMemcpy(ds->status_ptr, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess)
-    return ATTN_ERR_CUDA;
+    return cuda_failed();
   return value;
 }
 

@@ -34,6 +34,13 @@ int host_encode_bnhd(CUtensorMap* map, const void* ptr, int B, int N, int H, int
 // 4-D view (d, H, N, B) of a contiguous fp32 [B, N, H, d] tensor; box (d, 1, box_rows, 1).
 int host_encode_f32_bnhd(CUtensorMap* map, void* ptr, int B, int N, int H, int d, int box_rows);
 
+// What an entry point returns for a runtime call that failed.  The runtime keeps the error until it
+// is read; left there, the thread's next launch would be taken for a failed one.
+inline int cuda_failed() {
+  cudaGetLastError();
+  return ATTN_ERR_CUDA;
+}
+
 constexpr int kHostMaxDevices = 64;
 
 // Raise a kernel's dynamic shared-memory limit, once per device.
@@ -42,7 +49,7 @@ int host_raise_smem(const DeviceInfo& dev, int bytes) {
   static std::atomic<bool> done[kHostMaxDevices] = {};
   if (done[dev.device].load(std::memory_order_acquire)) return ATTN_OK;
   if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-    return ATTN_ERR_CUDA;
+    return cuda_failed();
   done[dev.device].store(true, std::memory_order_release);
   return ATTN_OK;
 }

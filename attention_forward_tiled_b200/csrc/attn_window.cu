@@ -63,7 +63,7 @@ size_t q4_bytes(int Hkv, int d, int num_blocks, int page_size) {
 
 bool dtype_ok(int dtype) { return dtype == ATTN_F16 || dtype == ATTN_BF16; }
 
-int launched() { return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
+int launched() { return cudaGetLastError() == cudaSuccess ? ATTN_OK : cuda_failed(); }
 
 constexpr int kMaxGridY = 65535;  // requests of a cache call
 
@@ -154,9 +154,9 @@ int take_workspace(const DeviceInfo& dev, void** ptr, size_t bytes, cudaStream_t
   static std::mutex mutex;
   static cudaMemPool_t pools[kHostMaxDevices] = {};
   cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(stream, &capturing) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (cudaStreamIsCapturing(stream, &capturing) != cudaSuccess) return cuda_failed();
   if (capturing != cudaStreamCaptureStatusNone)
-    return cudaMallocAsync(ptr, bytes, stream) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    return cudaMallocAsync(ptr, bytes, stream) == cudaSuccess ? ATTN_OK : cuda_failed();
   cudaMemPool_t pool = nullptr;
   {
     std::lock_guard<std::mutex> lock(mutex);
@@ -166,17 +166,17 @@ int take_workspace(const DeviceInfo& dev, void** ptr, size_t bytes, cudaStream_t
       props.location.type = cudaMemLocationTypeDevice;
       props.location.id = dev.device;
       cudaMemPool_t made = nullptr;
-      if (cudaMemPoolCreate(&made, &props) != cudaSuccess) return ATTN_ERR_CUDA;
+      if (cudaMemPoolCreate(&made, &props) != cudaSuccess) return cuda_failed();
       cuuint64_t keep = kPoolKeep;
       if (cudaMemPoolSetAttribute(made, cudaMemPoolAttrReleaseThreshold, &keep) != cudaSuccess) {
         cudaMemPoolDestroy(made);
-        return ATTN_ERR_CUDA;
+        return cuda_failed();
       }
       pools[dev.device] = made;
     }
     pool = pools[dev.device];
   }
-  return cudaMallocFromPoolAsync(ptr, bytes, pool, stream) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return cudaMallocFromPoolAsync(ptr, bytes, pool, stream) == cudaSuccess ? ATTN_OK : cuda_failed();
 }
 
 // One launch of the split-over-keys kernel; p holds what does not follow from the sizes.
@@ -204,7 +204,7 @@ int launch_split(const DeviceInfo& dev, SplitParams& p, cudaStream_t stream) {
   p.nonce = launch_nonce();
   attn_split_kernel<D, BF16, Q4, NT><<<slots, 256, C::kSmemBytes, stream>>>(p);
   int rc = launched();
-  if (cudaFreeAsync(ws, stream) != cudaSuccess) rc = ATTN_ERR_CUDA;
+  if (cudaFreeAsync(ws, stream) != cudaSuccess) rc = cuda_failed();
   return rc;
 }
 
@@ -319,22 +319,22 @@ int launch_window_bwd(const DeviceInfo& dev, const void* q, const void* k, const
     cfg.gridDim = dim3((unsigned)q_units);
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmemBytes;
-    if (cudaLaunchKernelEx(&cfg, attn_window_bwd_kernel<D, BF16, false>, pq) != cudaSuccess) rc = ATTN_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, attn_window_bwd_kernel<D, BF16, false>, pq) != cudaSuccess) rc = cuda_failed();
   }
   cfg.numAttrs = 1;
   if (rc == ATTN_OK) {
     cfg.gridDim = dim3((unsigned)(sink_units + rest_units));
     cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::kSmemBytes;
-    if (cudaLaunchKernelEx(&cfg, attn_window_bwd_kernel<D, BF16, true>, pk) != cudaSuccess) rc = ATTN_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, attn_window_bwd_kernel<D, BF16, true>, pk) != cudaSuccess) rc = cuda_failed();
   }
   if (rc == ATTN_OK && joined > 0) {
     cfg.gridDim = dim3((unsigned)(joined * kJoinBlocks));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
-    if (cudaLaunchKernelEx(&cfg, attn_window_bwd_join_kernel<D, BF16>, pk) != cudaSuccess) rc = ATTN_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, attn_window_bwd_join_kernel<D, BF16>, pk) != cudaSuccess) rc = cuda_failed();
   }
-  if (cudaFreeAsync(ws, stream) != cudaSuccess) rc = ATTN_ERR_CUDA;
+  if (cudaFreeAsync(ws, stream) != cudaSuccess) rc = cuda_failed();
   return rc;
 }
 
