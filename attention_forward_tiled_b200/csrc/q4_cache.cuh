@@ -61,17 +61,18 @@ struct Q4WriteParams {
   int B, Ln, Hkv, num_blocks, page_size, max_blocks;
 };
 
-// Code of x (finite) in a group: nearest even in the exact quotient.  2 (x - zero) against
-// (2 c + 1) scale in double: both sides are exact (fp16 and bf16 values span fewer than 53
-// bits here), so a tie is seen as one.
+// Code of x (finite) in a group: nearest even in the exact quotient.  2 x against
+// 2 zero + (2 c + 1) scale in double: x alone is exact whatever its exponent, and the right side,
+// made of fp16 values, is a multiple of 2^-24 below 2^19, so a tie is seen as one and nothing else is.
+// (x - zero would not be exact: a bf16 x of 2^-60 vanishes beside a zero of -1.)
 __device__ __forceinline__ int q4_code_exact(float x, float zero, float scale, float t) {
-  const double dx = 2.0 * ((double)x - (double)zero);
+  const double x2 = 2.0 * (double)x, zero2 = 2.0 * (double)zero;
   int c = (int)floorf(fminf(fmaxf(t, -1.f), 16.f) + 0.5f) - 1;  // one or two below the answer
   c = max(c, -2);
 #pragma unroll 1
   for (int i = 0; i < 4; ++i) {  // at most three borders lie between c and the answer
-    const double border = (double)(2 * c + 1) * (double)scale;
-    if (dx > border || (dx == border && (c & 1))) ++c;
+    const double border = fma((double)(2 * c + 1), (double)scale, zero2);
+    if (x2 > border || (x2 == border && (c & 1))) ++c;
     else break;
   }
   return min(max(c, 0), 15);
