@@ -341,8 +341,15 @@ ATTN_API int attn_topk(const float* score, int R, int P, int k, int* idx, attn_s
  *
  * k and v must be finite in every row, seen or not.  Calls with Nq * H / Hkv <= 32 (one
  * token of grouped heads, or a few) run split over the keys with a workspace taken
- * stream-ordered from a pool that keeps it between calls; others run the tiled kernel, where a bf16 V
- * element of magnitude 65536 or more records ATTN_ERR_RANGE as in attn_fwd.
+ * stream-ordered from a pool that keeps it between calls; others run the tiled kernel.
+ *
+ * Precision: scores, maxima, sums and lse are fp32; P enters P V rounded, O is rounded once.
+ * The tiled kernel has P and V in fp16, with attn_fwd's value range for bf16: a V element of
+ * magnitude 65536 or more (or inf, NaN) records ATTN_ERR_RANGE and leaves O undefined, elements
+ * below 2^-14 keep an absolute error under 2^-25, so outputs of that size lose bits.  Calls of
+ * up to 32 rows multiply bf16 V as it is, by P in two bf16 parts, and have neither limit.
+ * Against the rounding of O alone the error (root mean square) is 1.3 times in fp16 and 1.0
+ * in bf16.
  * Returns ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED or ATTN_ERR_CUDA;
  * asynchronous like attn_fwd.
  */
@@ -371,7 +378,7 @@ ATTN_API int attn_fwd_window(const void* q, const void* k, const void* v, void* 
  * than its own rounding, dk and dv by about 1.4 times theirs (root mean square).  In float16 both are
  * moved by powers of two taken from |dout|, |v| and D, so this holds for small and large dout and v
  * alike, as long as the gradients themselves lie in float16's normal range; queries whose dout is below
- * 2^-10 of the largest of the 128 around them add to dk with fewer bits.
+ * 2^-10 of the largest among those that see a key add to its dk with fewer bits.
  * Returns ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED or ATTN_ERR_CUDA;
  * asynchronous like attn_fwd.
  */
@@ -439,7 +446,7 @@ ATTN_API int attn_cache_read_q4(const void* cache, const int* block_table, const
  * seq_lens[b] keys; with causal = 1 token i stands at p = seq_lens[b] - Lq + i and sees keys
  * j <= p, and with window > 0 only those with j > p - window or j < sinks.  causal = 0: every
  * key (window must then be 0, unless Lq is 1).  Codes multiply on the tensor cores as they
- * are; scales and zeros are applied in fp32.  Cache rows past the sequence are not used, whatever
+ * are, against P times the scale in fp16 (two parts of it for fp16 outputs); zeros are applied in fp32.  Cache rows past the sequence are not used, whatever
  * they hold.  A token that sees no key gets O = 0 and lse = -inf.
  *
  *   q, out       [B, Lq, H, d]    dtype    (read / written)
