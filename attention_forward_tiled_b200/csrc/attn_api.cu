@@ -734,10 +734,6 @@ int host_encode_bnhd(CUtensorMap* map, const void* ptr, int B, int N, int H, int
   return encode_bnhd(map, ptr, B, N, H, d, dtype, box_rows, box_heads);
 }
 
-int host_encode_f32_bnhd(CUtensorMap* map, void* ptr, int B, int N, int H, int d, int box_rows) {
-  return encode_f32_bnhd(map, ptr, B, N, H, d, box_rows);
-}
-
 }  // namespace attn_b200
 
 extern "C" {

@@ -31,9 +31,6 @@ unsigned long long host_timeout_ns();
 int host_encode_bnhd(CUtensorMap* map, const void* ptr, int B, int N, int H, int d, int dtype,
                      int box_rows, int box_heads = 1);
 
-// 4-D view (d, H, N, B) of a contiguous fp32 [B, N, H, d] tensor; box (d, 1, box_rows, 1).
-int host_encode_f32_bnhd(CUtensorMap* map, void* ptr, int B, int N, int H, int d, int box_rows);
-
 // What an entry point returns for a runtime call that failed.  The runtime keeps the error until it
 // is read; left there, the thread's next launch would be taken for a failed one.
 inline int cuda_failed() {

@@ -67,7 +67,7 @@ int launched() { return cudaGetLastError() == cudaSuccess ? ATTN_OK : cuda_faile
 
 constexpr int kMaxGridY = 65535;  // requests of a cache call
 
-// Items of at most this many keys take a CTA each and no second launch.
+// Items of at most this many keys take a CTA each and no workspace.
 constexpr long long kDirectKeys = 512;
 
 // Calls f(head_dim, is bf16) with both as compile-time constants.
