@@ -89,10 +89,10 @@ __global__ void __launch_bounds__(256) q4_write_kernel(const Q4WriteParams p) {
   const int lane = threadIdx.x & 31, i = blockIdx.x * 8 + (threadIdx.x >> 5), b = blockIdx.y;
   if (i >= p.Ln) return;
   const long long most = (long long)p.max_blocks * p.page_size;
-  const long long len = min(max((long long)p.seq_lens[b], 0LL), most);
   const int n = p.new_lens ? min(max(p.new_lens[b], 0), p.Ln) : p.Ln;
-  const long long pos = len - n + i;
-  if (i >= n || pos < 0) return;
+  // a length past the table is not cut off here: its last tokens would land on earlier tokens' rows
+  const long long pos = (long long)max(p.seq_lens[b], 0) - n + i;
+  if (i >= n || pos < 0 || pos >= most) return;
   const int page = (int)(pos / p.page_size), in_page = (int)(pos - (long long)page * p.page_size);
   const int block = p.block_table[(long long)b * p.max_blocks + page];
   if (block < 0 || block >= p.num_blocks) return;  // never writes outside the cache, or another page

@@ -409,9 +409,10 @@ ATTN_API int attn_bwd_window(const void* q, const void* k, const void* v, const 
  *   new_lens     [B] int32 (DEVICE memory) or NULL: how many of the Ln tokens request b has
  *                (clamped to [0, Ln]; NULL: all).  Its tokens 0 .. n-1 become the last n
  *                positions of its sequence; the rest of its Ln rows are not read.
- *   page_size, max_blocks, num_blocks and the clamping of seq_lens as attn_fwd_decode_paged;
- *   k, v, cache 16-byte aligned; B <= 65535.  A token before position 0, or whose table entry lies outside
- *   [0, num_blocks), is not written.  Two requests of one call must not write to one page.
+ *   page_size, max_blocks and num_blocks as attn_fwd_decode_paged; k, v, cache 16-byte aligned;
+ *   B <= 65535.  A token before position 0, at or past the table's max_blocks * page_size positions,
+ *   or whose table entry lies outside [0, num_blocks), is not written.  Two requests of one call
+ *   must not write to one page.
  *
  * An element with no finite fp16 value (bf16 magnitude 65536 or more, inf, NaN) is stored as
  * +-65504 (NaN: -65504) and recorded as ATTN_ERR_RANGE in the status word.
