@@ -376,9 +376,10 @@ __global__ void __launch_bounds__(256, SplitCfg<D, Q4, NT>::kCtas)
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
       if (split_span<Q4>(p, b).n_tiles > 0) continue;
       uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (long long)b * p.Lq * p.H * D);
-      for (int e = threadIdx.x; e < p.Lq * p.H * (D / 4); e += 256) dst[e] = make_uint2(0u, 0u);
+      const long long rows = (long long)p.Lq * p.H;  // below 2^31, their elements are not
+      for (long long e = threadIdx.x; e < rows * (D / 4); e += 256) dst[e] = make_uint2(0u, 0u);
       if (p.lse != nullptr)
-        for (int e = threadIdx.x; e < p.Lq * p.H; e += 256) p.lse[(long long)b * p.H * p.Lq + e] = -INFINITY;
+        for (long long e = threadIdx.x; e < rows; e += 256) p.lse[(long long)b * p.H * p.Lq + e] = -INFINITY;
     }
     int longest;
     const long long total = split_total<D, Q4, NT>(p, longest);
