@@ -171,10 +171,10 @@ __device__ __forceinline__ SplitSpan split_span(const SplitParams& p, int b) {
   return s;
 }
 
-// Place in the chunks of all items end to end (requests, then their items): chunk `at` lies in
-// request b, whose items have n chunks each, the first of them at `begin`.
+// Place in the chunks of all items end to end (requests, then their items): a chunk of request b,
+// whose first item begins at `begin`.
 struct SplitPlace {
-  int b, n;
+  int b;
   long long begin;
 };
 
@@ -208,7 +208,7 @@ __device__ __forceinline__ SplitPlace split_find(const SplitParams& p, long long
   const int lane = threadIdx.x & 31;
   const long long per = (long long)p.Hkv * p.row_chunks;
   long long begin = 0;
-  SplitPlace place{p.B, 0, 0};
+  SplitPlace place{p.B, 0};
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int c = split_chunks<D, Q4, NT>(p, b0 + lane);
     const long long n = c * per;
@@ -222,7 +222,6 @@ __device__ __forceinline__ SplitPlace split_find(const SplitParams& p, long long
     if (past != 0) {
       const int l = __ffs(past) - 1;
       place.b = b0 + l;
-      place.n = __shfl_sync(0xffffffffu, c, l);
       place.begin = begin + __shfl_sync(0xffffffffu, sum - n, l);
       break;
     }
@@ -257,6 +256,8 @@ constexpr float kNoMax = -1e30f;
 // left by others passes for it once in 2^48), and the last part clears the word, so that a
 // replayed launch with the same nonce starts afresh.  So every part is counted in, those of a CTA
 // that gives up too: a count left behind would make the replay take an early part for the last.
+// (To count them in without the parts' loop took registers: 16 requests of 8000 to 16000 keys 112 ->
+// 114 us.)
 __device__ __forceinline__ bool split_arrive(unsigned long long* word, unsigned long long nonce, int n) {
   // the last part's guess is right at once, the others' time does not count
   unsigned long long seen = nonce | (unsigned long long)(n - 1);
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(256, SplitCfg<D, Q4, NT>::kCtas)
   // ---- the run of chunks of this CTA
   long long run = 0, run_end = 0, run_length = 1;
   int parts = 0;  // of an item (split_parts)
-  SplitPlace place{(int)(blockIdx.x / (p.Hkv * p.row_chunks)), 0, 0};
+  SplitPlace place{(int)(blockIdx.x / (p.Hkv * p.row_chunks)), 0};
   if (p.part != nullptr) {
     // rows of requests without keys, dealt to the CTAs in turn
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
@@ -434,7 +435,8 @@ __global__ void __launch_bounds__(256, SplitCfg<D, Q4, NT>::kCtas)
     const int all_from = span.n_sink + (low_max + 15) / 16 - span.first;
     const int all_end = span.n_sink + (pos_min + 1) / 16 - span.first;
     const int c0 = ca + warp;
-    const int mine = cb > c0 ? (cb - c0 + C::kWarps - 1) / C::kWarps : 0;  // chunks of this warp
+    // chunks of this warp; none once the CTA has given up, whose parts are still counted in (split_arrive)
+    const int mine = cb > c0 && !warp_flag(abort_flag) ? (cb - c0 + C::kWarps - 1) / C::kWarps : 0;
 
     // lane l: cache tile l % pieces of the warp's chunk (k / per_load) * per_load + l / pieces
     const uint8_t* piece = nullptr;
@@ -965,17 +967,8 @@ __global__ void __launch_bounds__(256, SplitCfg<D, Q4, NT>::kCtas)
     if (parts > 0) break;
     run += cb - ca;
     fence_proxy_async_smem();  // the partials' shared memory becomes the ring again
-    // one decision for the block: a warp alone that saw the abort would leave the others waiting
-    if (__syncthreads_or(run >= run_end || *abort_flag)) {
-      if (run < run_end && warp == 0) {
-        // given up: of the items left only the last can go on in other CTAs; its part here is counted in
-        const SplitPlace at = split_find<D, Q4, NT>(p, run_end - 1);
-        const long long x0 = run_end - 1 - (run_end - 1 - at.begin) % at.n;
-        if (lane == 0 && x0 + at.n > run_end)
-          split_arrive(p.arrived + blockIdx.x, p.nonce, (int)((x0 + at.n - 1) / run_length) - (int)blockIdx.x + 1);
-      }
-      break;
-    }
+    __syncthreads();
+    if (run >= run_end) break;
     if (run >= place.begin + (long long)n_chunks * p.Hkv * p.row_chunks) {  // the next request that has keys
       place.begin = run;
       do ++place.b;

@@ -46,26 +46,18 @@ def launch(items, run_length, words, gives_up=None, counts_in=True):
     order = list(range(len(runs)))
     random.Random(len(items) + run_length).shuffle(order)
 
-    def count(cta, item, joins):
-        x0, n = starts[item], items[item]
-        first = x0 // run_length
-        parts = (x0 + n - 1) // run_length - first + 1
-        arrived[item].add(cta)
-        if words.arrive(first, parts) and joins and len(arrived[item]) < parts:
-            early.append(item)
-
     for cta in order:
+        gone = False
         for at, (item, a, b) in enumerate(runs[cta]):
-            if (a, b) != (0, items[item]):
-                count(cta, item, True)
-            if gives_up == (cta, at):
-                run_end = min(total, (cta + 1) * run_length)
-                if counts_in and at + 1 < len(runs[cta]):
-                    # as the kernel finds it: the item of the run's last chunk, if it goes on past the run
-                    last = max(i for i, x in enumerate(starts) if x <= run_end - 1 and items[i])
-                    if starts[last] + items[last] > run_end:
-                        count(cta, last, False)
+            if gone and not counts_in:
                 break
+            if (a, b) != (0, items[item]):
+                x0, n = starts[item], items[item]
+                parts = (x0 + n - 1) // run_length - x0 // run_length + 1
+                arrived[item].add(cta)
+                if words.arrive(x0 // run_length, parts) and len(arrived[item]) < parts:
+                    early.append(item)
+            gone = gone or gives_up == (cta, at)
     return early
 
 
@@ -90,9 +82,10 @@ def test_parts_left_out_would_spoil_a_replay():
     assert any(words.values()) and launch(items, run_length, words)
 
 
-def test_the_kernel_counts_them_in():
+def test_the_kernel_goes_on_to_its_last_part():
+    """The loop over a run's parts ends with the run; giving up only leaves a part without chunks."""
     with open(os.path.join(abuild.CSRC, "split_sm100.cuh")) as f:
         text = f.read()
-    stop = text[text.index("if (__syncthreads_or(run >= run_end || *abort_flag))"):]
-    stop = stop[:stop.index("break;")]
-    assert re.search(r"split_arrive\(p\.arrived \+ blockIdx\.x", stop)
+    end = text[text.index("run += cb - ca;"):text.index("do ++place.b;")]
+    assert re.findall(r"if \((.*)\) break;", end) == ["run >= run_end"] and "abort" not in end
+    assert re.search(r"const int mine = cb > c0 && !warp_flag\(abort_flag\) \?", text)
