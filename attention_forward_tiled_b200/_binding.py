@@ -495,9 +495,10 @@ def attn_bwd_window(q, k, v, o, lse, dout, window, sinks=0, scale=None, stream=N
         raise ValueError(f"o must be a {tuple(q.shape)} tensor of {q.dtype} on {q.device}")
     strides = None
     if not o.is_contiguous():
-        if o.stride(3) != 1 or any(s % 8 for s in o.stride()[:3]):
+        steps = [s if n > 1 else 0 for s, n in zip(o.stride(), o.shape)]  # a dimension of one element takes none
+        if steps[3] != 1 or any(s % 8 for s in steps[:3]):
             raise ValueError("o must have contiguous channels and strides that are multiples of 8")
-        strides = (ctypes.c_longlong * 3)(*o.stride()[:3])
+        strides = (ctypes.c_longlong * 3)(*steps[:3])
     _check_buffer("dout", dout, q.shape, q.dtype, q.device)
     _check_buffer("lse", lse, (B, H, Nq), torch.float32, q.device)
     dq, dk, dv = _result_like("dq", dq, q), _result_like("dk", dk, k), _result_like("dv", dv, k)
