@@ -729,6 +729,8 @@ int host_device(DeviceInfo* out) {
 
 unsigned long long host_timeout_ns() { return g_timeout_ns.load(); }
 
+int host_inject() { return g_inject.load(); }
+
 int host_encode_bnhd(CUtensorMap* map, const void* ptr, int B, int N, int H, int d, int dtype, int box_rows,
                      int box_heads) {
   return encode_bnhd(map, ptr, B, N, H, d, dtype, box_rows, box_heads);

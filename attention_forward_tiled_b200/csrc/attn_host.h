@@ -26,6 +26,9 @@ int host_device(DeviceInfo* out);
 // Limit of every bounded device wait, as attn_debug_set left it.
 unsigned long long host_timeout_ns();
 
+// Fault to inject, as attn_debug_set left it (0: none).
+int host_inject();
+
 // 4-D view (d, H, N, B) of a contiguous 16-bit [B, N, H, d] tensor; box (64, box_heads,
 // box_rows, 1), 128-byte swizzle.
 int host_encode_bnhd(CUtensorMap* map, const void* ptr, int B, int N, int H, int d, int dtype,

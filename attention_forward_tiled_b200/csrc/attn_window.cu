@@ -114,6 +114,7 @@ int launch_window_fwd(const DeviceInfo& dev, const void* q, const void* k, const
   p.n_pairs = (Nq + 2 * rows - 1) / (2 * rows);
   p.scale_log2 = scale * 1.4426950408889634f;
   p.timeout_ns = host_timeout_ns();
+  p.inject = host_inject();
   const long long pairs = (long long)B * (H / pack) * p.n_pairs;
   // Units are of one size, so they end in a partial wave; when it would fill at most half of
   // the SMs (or there is no full one), its pairs run as units of one tile in about half the time.
@@ -256,6 +257,7 @@ int launch_window_bwd(const DeviceInfo& dev, const void* q, const void* k, const
   pq.scale = scale;
   pq.scale_log2 = scale * 1.4426950408889634f;
   pq.timeout_ns = host_timeout_ns();
+  pq.inject = pk.inject = host_inject();
   pk.lse = pq.lse; pk.status = pq.status;
   pk.B = B; pk.H = H; pk.Hkv = Hkv; pk.Nq = Nq; pk.Nk = Nk;
   pk.window = window; pk.sinks = sinks; pk.scale = scale; pk.scale_log2 = pq.scale_log2; pk.timeout_ns = pq.timeout_ns;
@@ -365,6 +367,7 @@ int attn_fwd_window(const void* q, const void* k, const void* v, void* out, floa
     p.B = B; p.H = H; p.Hkv = Hkv; p.Lq = Nq; p.Nk = Nk; p.causal = 1; p.window = window; p.sinks = sinks;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.timeout_ns = host_timeout_ns();
+    p.inject = host_inject();
     return launch_split_rows<D, BF16, false>(dev, p, st);
   });
 }
@@ -481,6 +484,7 @@ int attn_fwd_paged_q4(const void* q, const void* cache, const int* block_table, 
   p.num_blocks = num_blocks; p.page_size = page_size; p.max_blocks = max_blocks;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.timeout_ns = host_timeout_ns();
+  p.inject = host_inject();
   return by_type(d, dtype, [&](auto dim, auto bf16) { return launch_split_rows<dim(), bf16(), true>(dev, p, st); });
 }
 

@@ -66,6 +66,7 @@ struct SplitParams {
   unsigned long long nonce;     // of the launch, its low 16 bits 0
   float scale_log2;
   unsigned long long timeout_ns;
+  int inject;         // test hook: 1 = the first chunk of each CTA never counts as landed
 };
 
 template <int D, bool Q4, int NT>
@@ -356,7 +357,7 @@ __global__ void __launch_bounds__(256, SplitCfg<D, Q4, NT>::kCtas)
   const uint32_t ring = sbase + warp * C::kStages * C::kStageBytes;
   const uint32_t bars = sbase + C::kOffBar + warp * C::kStages * 8;
   if (lane == 0) {
-    for (int s = 0; s < C::kStages; ++s) mbar_init(bars + 8 * s, 1);
+    for (int s = 0; s < C::kStages; ++s) mbar_init(bars + 8 * s, p.inject == 1 && warp == 0 && s == 0 ? 2 : 1);
     mbar_init_fence();
   }
   if (threadIdx.x == 0) *abort_flag = 0;

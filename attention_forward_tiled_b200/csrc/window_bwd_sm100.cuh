@@ -80,6 +80,7 @@ struct WindowBwdParams {
   int sink_splits, splits;   // sink_splits units; the others' over splits
   float scale, scale_log2;
   unsigned long long timeout_ns;
+  int inject;                // test hook: 1 = the first tile X1 never counts as landed
 };
 
 template <int D>
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(WindowBwdCfg<D>::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(BAR(C::kBarXFull + i), 1);
+      mbar_init(BAR(C::kBarXFull + i), p.inject == 1 && i == 0 ? 2 : 1);
       // queries: D is taken from dO (X2) by the elementwise warps
       mbar_init(BAR(C::kBarXEmpty + i), !kKeys && i == 1 ? 1 + C::kEwWarps : 1);
       mbar_init(BAR(C::kBarUnitFull + i), 1);

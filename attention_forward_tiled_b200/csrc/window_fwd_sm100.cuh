@@ -49,6 +49,7 @@ struct WindowFwdParams {
   int n_split;       // the last n_split pair units run as two units of one tile each
   float scale_log2;  // scale * log2(e)
   unsigned long long timeout_ns;
+  int inject;        // test hook: 1 = the first Q tile never counts as landed
 };
 
 constexpr int kWindowUnitInts = 10;  // ints per published work unit (WindowUnit)
@@ -357,7 +358,7 @@ __global__ void __launch_bounds__(WindowFwdCfg<D>::kThreads, 1)
   // ---- one-time setup
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(BAR(C::kBarQFull + i), 1);
+      mbar_init(BAR(C::kBarQFull + i), p.inject == 1 && i == 0 ? 2 : 1);
       mbar_init(BAR(C::kBarQEmpty + i), 1);
       mbar_init(BAR(C::kBarSFull + i), 1);
       mbar_init(BAR(C::kBarSFree + i), 4);  // one arrive per softmax warp

@@ -484,8 +484,10 @@ ATTN_API int attn_version(void);
  *   wait_timeout_ns: limit of every bounded device wait (0 = default, 2 s).
  *   inject: 0 = off; 1 = the prefill producer skips its first Q-tile load, so
  *   the matrix-multiply issuer's wait on it expires, the kernel records
- *   ATTN_ERR_TIMEOUT and every role exits without trapping.  Applies to the
- *   calls that follow on this host process; returns ATTN_OK.
+ *   ATTN_ERR_TIMEOUT and every role exits without trapping; in attn_fwd_window,
+ *   attn_bwd_window and attn_fwd_paged_q4 the first tile that is loaded never
+ *   counts as landed, with the same end.  Applies to the calls that follow on
+ *   this host process; returns ATTN_OK.
  */
 ATTN_API int attn_debug_set(int inject, unsigned long long wait_timeout_ns);
 
