@@ -67,7 +67,12 @@ int launched() { return cudaGetLastError() == cudaSuccess ? ATTN_OK : cuda_faile
 
 constexpr int kMaxGridY = 65535;  // requests of a cache call
 
-// Items of at most this many keys take a CTA each and no workspace.
+// Items of at most this many keys take a CTA each and no workspace.  One token, 128 channels, dense
+// bf16 | 4-bit, parts or runs against a CTA an item (us, inputs not in L2): 4 items of 512 keys 12.9 / 10.2 |
+// 12.9 / 12.3, of 2048 17.0 / 18.4 | 17.0 / 20.5; 128 items of 512 17.0 / 14.3 | 17.0 / 12.3; 512 items of
+// 512 45.7 / 41.0 | 39.5 / 28.7.  Equal items of 1024 keys would still gain (4 items 14.9 / 12.3); the keys
+// counted here are the most that an item can have, and past some hundred a CTA with one of them would
+// work on while those of the short ones have ended.
 constexpr long long kDirectKeys = 512;
 
 // Calls f(head_dim, is bf16) with both as compile-time constants.
@@ -225,7 +230,11 @@ int launch_split_rows(const DeviceInfo& dev, SplitParams& p, cudaStream_t stream
   return launch_split<D, BF16, Q4, 2>(dev, p, stream);
 }
 
-// Steps of a unit of the keys' launch below which it is not split further.
+// Steps of a unit of the keys' launch below which it is not split further.  With 1, 2, 4, 8, 16 (us,
+// inputs not in L2, 2 heads of keys and groups of 4): 1000 tokens, window 256, 64 channels fp16 51.8 45.7
+// 39.5 45.6 58.0, 128 channels bf16 74.3 60.0 45.7 51.8 66.1; 700 tokens, every key, one head 43.6 35.4 37.5
+// 43.6 49.8; 2 x 512 tokens, 4 heads, window 128 78.4 66.1 60.0 57.9 58.0.  From 2000 tokens of 8 heads on
+// the share of an SM decides (150 to 156 with any).
 constexpr long long kBwdMinSteps = 4;
 
 template <int D, bool BF16>

@@ -241,7 +241,11 @@ __device__ __forceinline__ long long split_run(long long total, int grid, int mi
 // equal share of all chunks, but two or three parts.  So parts pay up to some chunks more than that share:
 // with 4 min_run (64) of them, one token over the cache, 32 heads over 8, 8 requests of 1500 to 3000
 // keys take 23.1 us against 30.4 in runs, 34 of 4500 to 6000 70.6 against 77.9; 16 of 40000 take
-// 187.8 in runs against 198.7 in parts.
+// 187.8 in runs against 198.7 in parts.  Chunks of other items, with 0, 4 and 16 min_run (inputs not in
+// L2): 4-bit, 8 requests of 1500 to 3000 keys, 16 rows 33.4 27.2 27.2, 32 rows 53.9 45.7 45.7; 5 of 500 to
+// 20000, 16 rows 49.8 49.8 55.9, 32 rows 94.8 94.8 115.3; 12 of 3000 to 9000, 16 rows 45.7 47.7 66.1; dense,
+// 4096 keys, 5 requests, 4 rows 33.4 31.3 29.3, 16 rows 39.5 33.4 35.4; 16 requests 64.1 62.0 62.0 and 70.2
+// 66.1 66.1.
 __device__ __forceinline__ int split_parts(long long total, int longest, long long items, int grid, int min_run) {
   const int most = (int)(grid / items);
   if (most == 0) return 0;

@@ -37,10 +37,11 @@
 // of P and in the subtraction of D; what they cost is the bounds (a small launch over V, and some 0.5 us a
 // unit): 4096 tokens in fp16 640 -> 667 us, 1000 tokens 37.2 -> 40.3.  bf16 has fp32's range and none of it.
 //
-// What bounds it, at 4096 tokens of 2 x 32 heads over 8, 128 channels, window 1024: the queries'
-// launch takes 327 us, the keys' 313, the join 6; the tensor cores work 40 and 46 % of that, the
+// What bounds it, at 4096 tokens of 2 x 32 heads over 8, 128 channels, window 1024, bf16: the queries'
+// launch takes 331 us, the keys' 316, the join 5; the tensor cores work 40 and 47 % of that, the
 // issue slots 36 and 29 %, DRAM 11 %.  A unit is 9 or 10 steps and about 5 us of them its start and
-// end (X1 and X2 have one buffer: two do not fit beside the ring), in which the tensor cores wait.
+// end (X1 and X2 have one buffer: two do not fit beside the ring at 128 channels; at 64 they would),
+// in which the tensor cores wait.
 //
 // Roles (576 threads): warps 0-15 elementwise and epilogue (four per TMEM lane quarter, 32 of the
 // 128 columns each), warp 16 producer, warp 17 MMA issuer.  Units are claimed with cluster launch

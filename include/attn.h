@@ -348,7 +348,7 @@ ATTN_API int attn_topk(const float* score, int R, int P, int k, int* idx, attn_s
  * magnitude 65536 or more (or inf, NaN) records ATTN_ERR_RANGE and leaves O undefined, elements
  * below 2^-14 keep an absolute error under 2^-25, so outputs of that size lose bits.  Calls of
  * up to 32 rows multiply bf16 V as it is, by P in two bf16 parts, and have neither limit.
- * Against the rounding of O alone the error (root mean square) is 1.3 times in fp16 and 1.0
+ * Against the rounding of O alone the error (root mean square) is 1.3 to 1.4 times in fp16 and 1.0
  * in bf16.
  * Returns ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED or ATTN_ERR_CUDA;
  * asynchronous like attn_fwd.
