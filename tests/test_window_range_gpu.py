@@ -99,3 +99,39 @@ def test_bf16_gradients_of_small_and_large_inputs(dout_size, v_size):
     few = v_size > 1.0
     q, k, v, dout = make(8 if few else 1, 4, 2, 16 if few else 500, 500, 128, "bf16", dout_size, v_size, 11)
     check(*gradients(q, k, v, dout, 200, 4), torch.bfloat16, limits=(1.05, 1.5, 1.5))
+
+
+def test_bounds_under_captured_graphs_and_streams():
+    """fp16 calls of very different sizes in two graphs and on two streams: each finds its own bounds."""
+    calls, want = [], []
+    for size, seed in ((1e-4, 1), (30.0, 2)):
+        q, k, v, dout = (t.cuda() for t in make(2, 4, 2, 300, 500, 128, "f16", size, 1.0, seed))
+        o, lse = attn.attn_fwd_window(q, k, v, 120, 4)
+        out = [torch.empty_like(t) for t in (q, k, v)]
+        calls.append(lambda a=(q, k, v, o, lse, dout), b=out, s=None: attn.attn_bwd_window(
+            *a, 120, 4, dq=b[0], dk=b[1], dv=b[2], stream=s))
+        want.append([t.clone() for t in calls[-1]()])
+
+    def check():
+        torch.cuda.synchronize()
+        assert attn.get_status() == 0
+        for call, w in zip(calls, want):
+            for got, x in zip(call.__defaults__[1], w):
+                assert torch.equal(got, x)
+                got.fill_(3.0)
+
+    check()
+    graphs = []
+    for call in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call()
+    for _ in range(3):
+        for graph in graphs:
+            graph.replay()
+        check()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(5):
+        for call, stream in zip(calls, streams):
+            call(s=stream)
+        check()
