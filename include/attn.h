@@ -369,8 +369,8 @@ ATTN_API int attn_fwd_window(const void* q, const void* k, const void* v, void* 
  *                    channels side by side), or NULL: o is contiguous
  *   k, v, dk, dv     [B, Nk, Hkv, d]   dtype    (dk, dv written)
  *   lse              [B, H, Nq]        float32  (read, required)
- *   Limits and alignment as attn_fwd_window; the outputs must not overlap each other or
- *   any input.  A row that sees no key has a zero gradient, and so has a key that no query
+ *   Limits and alignment as attn_fwd_window; q, k, v, o and dout finite in every row, seen or not;
+ *   the outputs must not overlap each other or any input.  A row that sees no key has a zero gradient, and so has a key that no query
  *   sees.  Every sum has a fixed order: equal calls give equal bits.  The workspace is taken
  *   stream-ordered from a pool that keeps up to 256 MiB between calls.
  *
