@@ -35,7 +35,7 @@
 // behind.  Typical products lie 2^4 to 2^8 below the bound, so P down to 2^-17 and rows of 2^-10 of the
 // largest still enter as normal numbers.  P enters dV as 2^12 P.  The powers of two ride in the exponent
 // of P and in the subtraction of D; what they cost is the bounds (a small launch over V, and some 0.5 us a
-// unit): 4096 tokens in fp16 640 -> 667 us, 1000 tokens 37.2 -> 40.3.  bf16 has fp32's range and none of it.
+// unit): 4096 tokens in fp16 641 -> 664 us, 1000 tokens 37.1 -> 40.5.  bf16 has fp32's range and none of it.
 //
 // What bounds it, at 4096 tokens of 2 x 32 heads over 8, 128 channels, window 1024, bf16: the queries'
 // launch takes 331 us, the keys' 316, the join 5; the tensor cores work 40 and 47 % of that, the
@@ -546,22 +546,25 @@ __global__ void __launch_bounds__(WindowBwdCfg<D>::kThreads, 1)
       if constexpr (!BF16) {
         const long long bh = (long long)u.b * p.Hkv + (kKeys ? u.h : u.h / G);
         const float* vm = p.vmax + bh * ((p.Nk + 127) / 128);
-        v_most = 0.f;
+        // Blocks of 128, one a lane; the first 32 are not looked at here, so that nobody waits for them.
         if constexpr (kKeys) {
           v_most = __ldcg(vm + u.x0 / 128);
-          g_most = d_most = 0.f;
-          const float2* qm = reinterpret_cast<const float2*>(p.qmax) + bh * ((p.Nq + 127) / 128);
-          const int last = (int)min((long long)p.Nq, u.a + 128LL * u.c) - 1;
-          for (int i = u.a / 128 + lane; i <= last / 128; i += 32) {
+          const float2* qm = reinterpret_cast<const float2*>(p.qmax) + bh * ((p.Nq + 127) / 128) + u.a / 128;
+          const int n = (int)((min((long long)p.Nq, u.a + 128LL * u.c) - 1) / 128) - u.a / 128 + 1;
+          const float2 first = lane < n ? __ldcg(qm + lane) : make_float2(0.f, 0.f);
+          g_most = first.x;
+          d_most = first.y;
+          for (int i = 32 + lane; i < n; i += 32) {
             const float2 w = __ldcg(qm + i);
             g_most = fmaxf(g_most, w.x);
             d_most = fmaxf(d_most, w.y);
           }
         } else {
-          // the sinks (rows of the stream below a), then keys from a + c on
-          const int last = (int)min((long long)p.Nk, 128LL * u.n + u.c) - 1;
-          for (int i = lane; i < (min(u.a, p.Nk) + 127) / 128; i += 32) v_most = fmaxf(v_most, __ldcg(vm + i));
-          for (int i = (u.a + u.c) / 128 + lane; i <= last / 128; i += 32) v_most = fmaxf(v_most, __ldcg(vm + i));
+          // the sinks' (rows of the stream below a), then those of the keys from a + c on
+          const int sinks = (min(u.a, p.Nk) + 127) / 128, from = (u.a + u.c) / 128 - sinks;
+          const int n = (int)((min((long long)p.Nk, 128LL * u.n + u.c) - 1) / 128) - from + 1;
+          v_most = lane < n ? __ldcg(vm + (lane < sinks ? lane : from + lane)) : 0.f;
+          for (int i = 32 + lane; i < n; i += 32) v_most = fmaxf(v_most, __ldcg(vm + (i < sinks ? i : from + i)));
         }
       }
       if constexpr (kKeys) {

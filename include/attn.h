@@ -370,9 +370,10 @@ ATTN_API int attn_fwd_window(const void* q, const void* k, const void* v, void* 
  *   k, v, dk, dv     [B, Nk, Hkv, d]   dtype    (dk, dv written)
  *   lse              [B, H, Nq]        float32  (read, required)
  *   Limits and alignment as attn_fwd_window; q, k, v, o and dout finite in every row, seen or not;
- *   the outputs must not overlap each other or any input.  A row that sees no key has a zero gradient, and so has a key that no query
- *   sees.  Every sum has a fixed order: equal calls give equal bits.  The workspace is taken
- *   stream-ordered from a pool that keeps up to 256 MiB between calls.
+ *   the outputs must not overlap each other or any input.  A row that sees no key has a zero
+ *   gradient, and so has a key that no query sees.  Every sum has a fixed order: equal calls give
+ *   equal bits.  The workspace is taken stream-ordered from a pool that keeps up to 256 MiB
+ *   between calls.
  *
  * P and dS enter their products rounded to dtype, dS of dQ in two parts: dq is off by little more
  * than its own rounding, dk and dv by about 1.4 times theirs (root mean square).  In float16 both are
